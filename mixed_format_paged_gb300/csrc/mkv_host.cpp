@@ -1042,12 +1042,13 @@ mkv_status mkv_seq_truncate(mkv_pool* p, int32_t n, const int32_t* ids, const in
       list.push_back({p->seqs[own[i].first].pages[own[i].second].slot, p->free_fp8[p->free_fp8.size() - 1 - i], 0, len % P});
     }
     if ((st = enqueue_page_copies(p, p, list, reinterpret_cast<cudaStream_t>(stream))) != MKV_OK) return st;
+    // the slots that were copied to, all of them off the free list before the first old slot may go back on it
+    p->free_fp8.resize(p->free_fp8.size() - own.size());
     for (size_t i = 0; i < own.size(); ++i) {
-      PageRec& r = p->seqs[own[i].first].pages[own[i].second];
-      const int32_t was = r.slot;
-      r.slot = take_fp8(p);
-      drop_ref(p, false, was);
+      p->seqs[own[i].first].pages[own[i].second].slot = list[i].dst;
+      p->ref_fp8[list[i].dst] = 1;
     }
+    for (const PageCopy& c : list) drop_ref(p, false, c.src);
     for (int i = 0; i < n; ++i) {
       SeqRec& s = p->seqs[ids[i]];
       s.len = new_len[i];

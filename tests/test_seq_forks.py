@@ -403,3 +403,121 @@ def test_calls_that_the_host_plans_refuse_a_capture(mkv):
     pool.truncate([1], [130])
     for r in range(2):
         assert all(torch.equal(x, y) for x, y in zip(want[r], _dense(pool, 0, r)))
+
+
+# ------------------------------------------------------------------ several owners of shared pages in one truncation
+def _cut_rows(mkv, pool, ids, lens):
+    """Truncate and check the page records: full pages stay where they were, and a page that was shared and became
+    partial lies in a slot that was free before the call, one that nobody else has."""
+    n = pool.cfg.max_seqs
+    before = {i: _slots(pool, i) for i in range(n)}
+    P = pool.cfg.page_size
+    in_use = {s for i in range(n) for t, s in before[i] if t != 3}
+    owners = {s: sum(s == b for i in range(n) for t, b in before[i] if t != 3) for s in in_use}
+    pool.truncate(ids, lens)
+    for i in range(n):
+        after = _slots(pool, i)
+        if i not in ids:
+            assert after == before[i]
+            continue
+        m = lens[ids.index(i)]
+        assert after[:m // P] == before[i][:m // P] and len(after) == -(-m // P)
+        if m % P:
+            was, now = before[i][m // P][1], after[m // P][1]
+            if owners[was] > 1:
+                assert now not in in_use, f"sequence {i}: slot {now} held another page when its rows were copied"
+            else:
+                assert now == was
+    used = [s for i in range(n) for t, s in _slots(pool, i) if t != 3]
+    assert len(set(used)) == pool.cfg.fp8_slots - pool.stats().fp8_slots_free
+    tails = [_slots(pool, i)[-1][1] for i in range(n) if pool.seq_info(i)[0] % P]
+    assert all(used.count(s) == 1 for s in tails)
+
+
+@pytest.mark.parametrize("order", [[0, 1, 2], [0, 2, 1], [1, 0, 3, 2], [0, 1, 2, 3], [3, 2, 1, 0]])
+def test_truncating_all_owners_of_several_shared_pages(mkv, order):
+    p = _host(mkv)
+    p.extend([0, 2], [128, 128])
+    p.fork([0, 2], [1, 3])
+    _cut_rows(mkv, p, order, [69] * len(order))
+    for i in range(4):
+        p.release(i)
+    assert p.stats().fp8_slots_free == 12
+
+
+def test_random_truncations_of_several_sequences_a_call(mkv):
+    rng = np.random.default_rng(11)
+    cut = 0
+    for _ in range(60):
+        p = _host(mkv, fp8_slots=60, max_seqs=12)
+        roots = [int(x) for x in rng.permutation(12)[:3]]
+        p.extend(roots, [int(x) for x in rng.integers(1, 64 * 5, 3)])
+        for i in range(12):
+            if i not in roots and rng.random() < 0.8:
+                p.fork([roots[int(rng.integers(0, 3))]], [i])
+        for _ in range(4):
+            ids = [int(x) for x in rng.permutation(12)[:int(rng.integers(1, 13))]]
+            lens = [int(rng.integers(0, p.seq_info(i)[0] + 1)) for i in ids]
+            try:
+                _cut_rows(mkv, p, ids, lens)
+            except mkv.MkvError as e:
+                assert e.status == 3
+                continue
+            cut += 1
+    assert cut > 100
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("order", [[0, 1, 2, 3, 4, 5], [1, 0, 3, 2, 5, 4], [0, 2, 4, 1, 3, 5]])
+def test_truncated_owners_of_several_shared_pages_hold_their_own_rows(mkv, order):
+    pool, _ = _fill(mkv, lens=(3 * 64, 2 * 64, 2 * 64 + 9))
+    want = {(l, r): _dense(pool, l, r) for l in range(3) for r in range(3)}
+    pool.fork([0, 1, 2], [3, 4, 5])
+    lens = [64 + 7 + 3 * r for r in range(6)]
+    pool.truncate([(i % 3) + 3 * (i // 3) for i in order], [lens[i] for i in order])
+    for layer in range(3):
+        for r in range(6):
+            for a, b in zip(_dense(pool, layer, r), want[layer, r % 3]):
+                assert torch.equal(a, b[:lens[r]]), (layer, r)
+
+
+@pytest.mark.gpu
+def test_random_forks_and_batched_truncations_keep_every_sequences_rows(mkv):
+    """A model of the contents: each sequence's rows are a prefix of its ancestor's followed by rows of its own."""
+    rng = np.random.default_rng(5)
+    pool, g = _fill(mkv, layers=2, fp8=64, lens=(200, 150, 128), seqs=8)
+    rows = {r: [_dense(pool, layer, r) for layer in range(2)] for r in range(3)}
+    for step in range(40):
+        live = [r for r in range(8) if pool.seq_info(r)[0]]
+        empty = [r for r in range(8) if not pool.seq_info(r)[0]]
+        op = int(rng.integers(0, 4))
+        if op == 0 and live and empty:
+            src = [live[int(rng.integers(0, len(live)))] for _ in empty]
+            pool.fork(src, empty)
+            for s, d in zip(src, empty):
+                rows[d] = [list(x) for x in rows[s]]
+        elif op == 1 and live:
+            ids = [int(x) for x in rng.permutation(live)[:4]]
+            add = [int(x) for x in rng.integers(1, 40, len(ids))]
+            if any(pool.seq_info(i)[0] + n > 64 * 8 for i, n in zip(ids, add)):
+                continue
+            pool.extend(ids, add)
+            for layer in range(2):
+                k, v = (torch.randn(sum(add), 4, 256, generator=g).to(DEV) for _ in range(2))
+                pool.append(layer, ids, add, k, v)
+                for i, n in zip(ids, add):
+                    new = _dense(pool, layer, i)
+                    for old, x in zip(rows[i][layer], new):
+                        assert torch.equal(x[:old.shape[0]], old), (step, layer, i)
+                    rows[i][layer] = new
+        elif live:
+            ids = [int(x) for x in rng.permutation(live)]
+            lens = [int(rng.integers(1, pool.seq_info(i)[0] + 1)) for i in ids]
+            pool.truncate(ids, lens)
+            for i, n in zip(ids, lens):
+                rows[i] = [[x[:n] for x in kv] for kv in rows[i]]
+        for r in range(8):
+            if pool.seq_info(r)[0]:
+                for layer in range(2):
+                    for a, b in zip(_dense(pool, layer, r), rows[r][layer]):
+                        assert torch.equal(a, b), (step, layer, r)
