@@ -180,10 +180,9 @@ _INT = {int}
 def _i32(values):
     """int32 C array of `values` (small arrays are cached: the same batch is
     passed for every layer of a decode step)."""
-    if set(map(type, values)) <= _INT:       # (the usual case, twice as fast)
-        key = tuple(values)
-    else:
-        key = tuple(int(v) for v in values)
+    key = tuple(values)                      # (once: it may be an iterator)
+    if not set(map(type, key)) <= _INT:      # (twice as fast as converting what is an int already)
+        key = tuple(int(v) for v in key)
     hit = _I32_CACHE.get(key)
     if hit is None:
         hit = ((ctypes.c_int32 * max(1, len(key)))(*key), len(key))

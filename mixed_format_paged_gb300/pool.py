@@ -74,6 +74,7 @@ class MkvPool:
         """Append with rotary positions in one launch (mkv_append_rope): k is
         rotated at its tokens' positions and quantised, v quantised, q
         [sum n_new, H_q, d] rotated.  Returns the rotated q (None without q)."""
+        n_new = list(n_new)
         T, d = int(sum(n_new)), self.head_dim
         if q is None and q_out is not None:
             raise ValueError("q_out without q")

@@ -521,3 +521,36 @@ def test_random_forks_and_batched_truncations_keep_every_sequences_rows(mkv):
                 for layer in range(2):
                     for a, b in zip(_dense(pool, layer, r), rows[r][layer]):
                         assert torch.equal(a, b), (step, layer, r)
+
+
+# ------------------------------------------------------------------ ids and counts as one-shot iterators
+def test_iterators_and_arrays_name_the_same_batches_as_lists(mkv):
+    forms = [list, tuple, iter, lambda x: (i for i in x), lambda x: map(int, x), np.array, torch.tensor]
+    for form in forms:
+        p = _host(mkv)
+        p.extend(form([0, 1]), form([70, 64]))
+        assert p.seq_info(0) == (70, 2) and p.seq_info(1) == (64, 1), form
+        p.fork(form([0, 0]), form([2, 3]))
+        assert p.seq_info(3) == (70, 2)
+        p.truncate(form([2, 3]), form([3, 65]))
+        assert p.seq_info(2) == (3, 1) and p.seq_info(3) == (65, 2)
+        q = _host(mkv)
+        q.copy_from(p, form([3]), form([5]))
+        assert q.seq_info(5) == (65, 2)
+        p.demote(form([0]), form([0]))
+        assert p.page_info(0, 0)[0] == 3
+
+
+@pytest.mark.gpu
+def test_appends_of_iterators_write_what_lists_write(mkv):
+    from mixed_format_paged_gb300 import Rope
+    rope, got = Rope(128), []
+    for form in (list, iter):
+        pool, g = _fill(mkv, lens=())
+        q, k, v = (torch.randn(75, h, 256, generator=g).to(DEV) for h in (24, 4, 4))
+        pool.extend(form([0, 1]), form([70, 5]))
+        pool.append(0, form([0, 1]), form([70, 5]), k, v)
+        out = pool.append_rope(1, form([0, 1]), form([70, 5]), q, k, v, rope)
+        got.append([out] + [x for layer in range(2) for r in range(2) for x in _dense(pool, layer, r)])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
