@@ -267,7 +267,9 @@ typedef enum {
   MKV_ROPE_NTK = 2,        /* base * factor^(rot_dim / (rot_dim - 2)) */
   MKV_ROPE_YARN = 3,       /* Peng et al. 2023: w / factor for the slow pairs (fewer than beta_slow turns over
                               original_length), w for the fast ones (more than beta_fast), a linear ramp over the
-                              pair index between; m = 0.1 ln(factor) + 1 */
+                              pair index between (from the pair of beta_fast turns, rounded down, to that of beta_slow,
+                              rounded up, which may lie past the last one; both within 0 .. rot_dim - 1);
+                              m = 0.1 ln(factor) + 1 */
   MKV_ROPE_WAVELENGTH = 4  /* w / factor for pairs of fewer than low_freq turns over original_length, w for more
                               than high_freq, between them a blend linear in the number of turns */
 } mkv_rope_scaling;

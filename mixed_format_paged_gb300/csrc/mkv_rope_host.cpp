@@ -89,8 +89,9 @@ mkv_status mkv_rope_init(const mkv_rope_config* c, mkv_rope_table* table) {
     auto at = [&](double turns) {
       return r * std::log(c->original_length / (turns * 2.0 * M_PI)) / (2.0 * std::log(c->base));
     };
+    // (the ramp may end past the last pair, which then turns too fast to be slowed down by the whole factor)
     const double low = std::fmax(std::floor(at(c->beta_fast)), 0.0);
-    const double high = std::fmin(std::ceil(at(c->beta_slow)), half - 1.0);
+    const double high = std::fmin(std::ceil(at(c->beta_slow)), r - 1.0);
     for (int i = 0; i < half; ++i) {
       const double slow = std::fmin(std::fmax((i - low) / std::fmax(high - low, 1e-3), 0.0), 1.0);
       w[i] = w[i] / c->factor * slow + w[i] * (1.0 - slow);

@@ -60,6 +60,24 @@ def test_yarn_keeps_fast_pairs_divides_slow_ones_and_scales(mkv):
     assert np.isclose(yarn.mscale, 0.1 * math.log(f) + 1, rtol=1e-7)
 
 
+@pytest.mark.parametrize("rot,base,L,f", [
+    (128, 1e4, 131072, 4.0), (128, 1e4, 65536, 4.0), (64, 1e4, 131072, 8.0), (256, 1e4, 262144, 2.0), (4, 1e6, 32768, 4.0),
+    (2, 1e4, 4096, 4.0), (128, 500.0, 1 << 20, 4.0), (6, 100.0, 1e9, 4.0), (128, 1e6, 32768, 4.0), (64, 1e4, 100, 2.0),
+])
+def test_yarn_ramp_may_end_past_the_last_pair(mkv, rot, base, L, f):
+    # in 64-bit numpy; the library's own fp64 differs by a few roundings (2^-53 each) of logs, powers and products
+    fast, slow = 32.0, 1.0
+    w = base ** (-np.arange(0, rot, 2) / rot)
+    index = lambda turns: rot / 2 * math.log(L / (2 * math.pi * turns)) / math.log(base)    # pair of that many turns
+    lo, hi = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), rot - 1)
+    ramp = np.clip((np.arange(rot // 2) - lo) / max(hi - lo, 1e-3), 0, 1)
+    got = mkv.Rope(rot, base=base, scaling="yarn", factor=f, original_length=L, beta_fast=fast, beta_slow=slow).inv_freq
+    assert np.allclose(got, w * (1 - ramp) + w / f * ramp, rtol=1e-12, atol=0)
+    for a, b in zip(w, got):        # only pairs of fewer than beta_slow turns take the whole factor
+        if L * a / (2 * math.pi) > slow and index(slow) < rot - 1:
+            assert b > a / f * (1 + 1e-9)
+
+
 def test_wavelength_scaling_blends_by_turns(mkv):
     L, f, lo, hi = 8192, 8.0, 1.0, 4.0
     plain = mkv.Rope(128, base=5e5)
