@@ -578,8 +578,9 @@ mkv_status mkv_step_graph_destroy(mkv_step_graph* graph);
  *   num_pages, H_kv] fp32; value = code * scale.
  * mkv_blk8_append writes scales that are powers of two (0 for a page of zeros):
  * s = 2^e, e the smallest integer >= -126 with max |x| <= 448 * 2^e over the
- * tokens that the page has held since its position 0 was written, and code =
- * e4m3_rn(x / s).  When a later token raises e, the page's codes are brought to
+ * finite values of the tokens that the page has held since its position 0 was
+ * written, and code = e4m3_rn(x / s), NaN for a NaN or an infinity (the attention
+ * of every query token that sees it is then NaN).  When a later token raises e, the page's codes are brought to
  * the new scale, which is exact except for codes that fall into E4M3's
  * subnormals (rounded to nearest even).  The attention takes any scale >= 0.
  *
@@ -631,8 +632,7 @@ mkv_status mkv_blk8_append(mkv_blk8* cache, int32_t layer, int32_t n, int32_t to
  * `dtype` (MKV_BF16 or MKV_F16), contiguous; lse: fp32 [n, nq, H_q] (natural log,
  * of scores times softmax_scale).  A query token that sees nothing (lens[b] <
  * nq - i) gets out 0 and lse -infinity.  Codes at positions past a sequence's
- * end are ignored, whatever they hold, and a NaN code (which append writes for a
- * NaN alone) reaches only the query tokens that see its token.  Scores, sums and accumulators are fp32; q
+ * end are ignored, whatever they hold, and a NaN code reaches only the query tokens that see its token.  Scores, sums and accumulators are fp32; q
  * enters exactly (elements below 2^-17 of their row's largest: to 2^-23 of it),
  * softmax weights with 8 significant bits (11 for MKV_F16), down to 2^-16 (2^-20)
  * of the largest weight so far times its page's scale.  The result does not

@@ -5,6 +5,8 @@
 // e4m3_rn(x / s).  Dividing by a power of two is exact, so a code is rounded once, whatever the order in
 // which the tokens came; when a new token raises e, the older codes are brought to the new scale, which is
 // exact too except where a code falls into e4m3's subnormals (then it is rounded, to nearest even).
+// e4m3 has no infinity, and a scale for one would erase the page's other values: infinities become NaN codes, as NaNs
+// do, and the maximum is that of the finite values (taken again, from shared memory, by a page that met one).
 //
 // Bound: memory, the rows in and the codes out.  A page's rows stay in shared memory between the maximum and
 // the codes, so they are read once; asynchronous copies bring them there, each thread its own 64 values (no
@@ -91,7 +93,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Exponent field of the scale (0: scale 0) for a largest magnitude: 448 = 1.75 * 2^8.
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
+// Exponent field of the scale (0: scale 0) for a largest magnitude (finite): 448 = 1.75 * 2^8.
 __device__ __forceinline__ int scale_exponent(float amax) {
   if (!(amax > 0.f)) return 0;
   int x;
@@ -167,6 +170,25 @@ mkv_blk8_append_kernel(const __grid_constant__ B8AppendParams p) {
   amax = warp_max[threadIdx.x & (THREADS / 32 - 1)];
 #pragma unroll
   for (int o = THREADS / 64; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+  const bool inf = amax == INFINITY;                    // (of the whole block)
+  if (inf) {                                            // the scale is that of the finite values
+    amax = 0.f;
+#pragma unroll 1
+    for (int j = 0; j < 8 && j * rows < work; ++j) {
+      float y[8];
+      get8(stage + j * THREADS * 8, y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, finite(y[i]) ? fabsf(y[i]) : 0.f);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+    __syncthreads();                                    // every thread has read the first maxima
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = amax;
+    __syncthreads();
+    amax = warp_max[threadIdx.x & (THREADS / 32 - 1)];
+#pragma unroll
+    for (int o = THREADS / 64; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+  }
   const int want = scale_exponent(amax);
   const float now = fmaxf(was, pow2_field(want));
   // 1 / now: the reciprocal of a power of two (2^-126 .. 2^121) is one
@@ -199,6 +221,10 @@ mkv_blk8_append_kernel(const __grid_constant__ B8AppendParams p) {
     if (j * rows >= work) break;
     float y[8];
     get8(stage + j * THREADS * 8, y);
+    if (inf) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = finite(y[i]) ? y[i] : NAN;
+    }
     uint2 w;
     w.x = e4m3x2(y[0] * inv, y[1] * inv) | (e4m3x2(y[2] * inv, y[3] * inv) << 16);
     w.y = e4m3x2(y[4] * inv, y[5] * inv) | (e4m3x2(y[6] * inv, y[7] * inv) << 16);
