@@ -373,7 +373,7 @@ __device__ __forceinline__ void fp8_quantize_fast(const float (&x)[8], uint32_t 
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
   amax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(amax)));   // (not negative: ordered as integers)
-  s16 = __float2half_rn(quotient(amax, 448.0f, 1.0f / 448.0f));
+  s16 = __float2half_rn(amax < INFINITY ? quotient(amax, 448.0f, 1.0f / 448.0f) : amax);   // (inf - inf is no remainder)
   float s = __half2float(s16), r = 0.f;
   if (s < INFINITY && s != 0.f) r = __frcp_rn(s);
   else s = 0.f;                                          // a scale of 0, or past fp16's range: quotients and codes 0

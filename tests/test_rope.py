@@ -361,6 +361,36 @@ def test_append_rope_quantises_as_append_does_at_every_magnitude(mkv, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [70, 3000])
+def test_append_rope_quantises_infinities_and_nans_as_append_does(mkv, n, dtype):
+    """Rows with an infinity (scale infinity), with a NaN (the scale of the others), with both, at both launch shapes."""
+    g = torch.Generator().manual_seed(10)
+    k = torch.randn(n, 4, 256, generator=g)
+    k[3, 0, 7] = math.inf                                 # (not in the rotated pair, whose other value it would reach)
+    k[5, 1, 255] = -math.inf
+    k[6, 2, 100] = math.nan
+    k[7, 3, 9], k[7, 3, 200] = math.inf, math.nan
+    k[8, 0, 2:] = math.inf
+    k[9, 1, 2:] = math.nan
+    k, v = k.to(dtype).to(DEV), k.flip(0).to(dtype).contiguous().to(DEV)
+    rope = mkv.Rope(2, inv_freq=[0.0])                    # the identity
+    pools = [mkv.MkvPool(1, 24, 4, 256, 64, 60, 1, max_seqs=1, max_pages_per_seq=60, device=DEV) for _ in range(2)]
+    for pool in pools:
+        pool.extend([0], [n])
+    pools[0].append(0, [0], [n], k, v)
+    pools[1].append_rope(0, [0], [n], None, k, v, rope)
+    for pg in range(pools[0].seq_info(0)[1]):
+        a, b = (np.frombuffer(p.export_page(0, 0, pg)[0], np.uint8).reshape(4, 2, 64 * 258) for p in pools)
+        scales = [x[:, :, 64 * 256:].copy().view(np.uint16) for x in (a, b)]
+        assert (scales[0] == scales[1]).all(), pg
+        # codes: bits, but for the sign of a zero (see above) and of a NaN
+        bad = np.flatnonzero(a != b)
+        a, b = a.reshape(-1)[bad], b.reshape(-1)[bad]
+        assert ((a & 0x7F) == (b & 0x7F)).all() and np.isin(a & 0x7F, [0, 0x7F]).all(), pg
+
+
+@pytest.mark.gpu
 def test_append_rope_decode_step_against_the_definition(mkv):
     """Rotate, append and attend, as a decode loop does, against fp64 attention over the exported pages' values and
     the formula's q."""
