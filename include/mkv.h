@@ -616,7 +616,9 @@ mkv_status mkv_blk8_destroy(mkv_blk8* cache);
 
 /* Append tokens of one layer: sequence i gets rows cu_new[i] .. cu_new[i + 1] - 1
  * (device int32 [n + 1], cu_new[0] = 0, not decreasing, ends at `tokens`) as its
- * last tokens; lens[i] counts them already.  k, v: [tokens, H_kv, d] of `dtype`
+ * last tokens; lens[i] counts them already.  (Offsets outside 0 .. tokens or falling, or
+ * more new tokens than lens[i], set the error word; nothing is written for that
+ * sequence.)  k, v: [tokens, H_kv, d] of `dtype`
  * (MKV_F32, MKV_BF16, MKV_F16), dims contiguous, token and head strides in
  * elements (multiples of 16 bytes, addresses 16-byte aligned; head strides >= d
  * or tokens' -- inputs may overlap).  No two sequences of a call may write one

@@ -125,11 +125,11 @@ mkv_blk8_append_kernel(const __grid_constant__ B8AppendParams p) {
     below += __syncthreads_count(i < p.n && p.cu[min(i, p.n - 1)] / p.P + 2 * i <= x);
   }
   const int r = max(below, 1) - 1;
-  const int c0 = p.cu[r], len = p.lens[r];
-  const int add = min(p.cu[r + 1], p.tokens) - c0;
+  const int c0 = p.cu[r], c1 = p.cu[r + 1], len = p.lens[r];
+  const int add = c1 - c0;
   const int old = len - add;
-  if (add <= 0) return;
-  if (c0 < 0 || old < 0) {                              // more new tokens than the sequence holds
+  if (c1 == c0) return;
+  if (c0 < 0 || c1 < c0 || c1 > p.tokens || old < 0) {  // rows that are not there, or more of them than the sequence holds
     if (threadIdx.x == 0) atomicOr(p.err, kErrBadPage);
     return;
   }
