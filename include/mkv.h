@@ -580,9 +580,13 @@ mkv_status mkv_step_graph_destroy(mkv_step_graph* graph);
  * s = 2^e, e the smallest integer >= -126 with max |x| <= 448 * 2^e over the
  * finite values of the tokens that the page has held since its position 0 was
  * written, and code = e4m3_rn(x / s), NaN for a NaN or an infinity (the attention
- * of every query token that sees it is then NaN).  When a later token raises e, the page's codes are brought to
- * the new scale, which is exact except for codes that fall into E4M3's
- * subnormals (rounded to nearest even).  The attention takes any scale >= 0.
+ * of every query token that sees it is then NaN).  When a later token raises e,
+ * the page's codes are brought to the new scale, which is exact except for codes
+ * that fall into E4M3's subnormals (rounded to nearest even).  The attention
+ * takes any finite scale >= 0.  So does an append into a page whose codes and
+ * scale the program filled in itself: it keeps that scale until a token raises it
+ * to a power of two (the older codes are then rounded again), and code =
+ * e4m3_rn(fp32_rn(x / s)).
  *
  * `table` [n, table_width] int32 (device): page ids of each sequence, logical
  * page by logical page; entries past a sequence's last page are not read.

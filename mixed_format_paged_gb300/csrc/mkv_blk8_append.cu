@@ -191,8 +191,10 @@ mkv_blk8_append_kernel(const __grid_constant__ B8AppendParams p) {
   }
   const int want = scale_exponent(amax);
   const float now = fmaxf(was, pow2_field(want));
-  // 1 / now: the reciprocal of a power of two (2^-126 .. 2^121) is one
+  // 1 / now: the reciprocal of a power of two (2^-126 .. 2^121) is one; a scale that a program filled in itself may be
+  // anything, and then the codes are of correctly rounded quotients
   const float inv = now > 0.f ? __frcp_rn(now) : 0.f;
+  const bool odd = __float_as_uint(now) & 0x007fffffu;
   __syncthreads();                                      // every thread has read the old scale
   if (threadIdx.x == 0 && (now != was || t0 == 0)) p.scale[kv][cell] = now;
   if (now > was && was > 0.f) {                         // bring the page's older codes to the new scale
@@ -225,9 +227,16 @@ mkv_blk8_append_kernel(const __grid_constant__ B8AppendParams p) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = finite(y[i]) ? y[i] : NAN;
     }
+    if (odd) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(y[i], now);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] *= inv;
+    }
     uint2 w;
-    w.x = e4m3x2(y[0] * inv, y[1] * inv) | (e4m3x2(y[2] * inv, y[3] * inv) << 16);
-    w.y = e4m3x2(y[4] * inv, y[5] * inv) | (e4m3x2(y[6] * inv, y[7] * inv) << 16);
+    w.x = e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16);
+    w.y = e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16);
     reinterpret_cast<uint2*>(codes)[(t0 << shift) + threadIdx.x + j * THREADS] = w;
   }
 }
