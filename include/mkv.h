@@ -638,7 +638,9 @@ mkv_status mkv_blk8_append(mkv_blk8* cache, int32_t layer, int32_t n, int32_t to
  * `dtype` (MKV_BF16 or MKV_F16), contiguous; lse: fp32 [n, nq, H_q] (natural log,
  * of scores times softmax_scale).  A query token that sees nothing (lens[b] <
  * nq - i) gets out 0 and lse -infinity.  Codes at positions past a sequence's
- * end are ignored, whatever they hold, and a NaN code reaches only the query tokens that see its token.  Scores, sums and accumulators are fp32; q
+ * end are ignored, whatever they hold, and a NaN code reaches only the query tokens that see its token.  A
+ * query row (token and head) with a NaN or an infinity that sees a token gets NaN, in out and lse, and so does
+ * one with a score above fp32's range, or with none above -1e30 (in units of log 2).  Scores, sums and accumulators are fp32; q
  * enters exactly (elements below 2^-17 of their row's largest: to 2^-23 of it),
  * softmax weights with 8 significant bits (11 for MKV_F16), down to 2^-16 (2^-20)
  * of the largest weight so far times its page's scale.  The result does not

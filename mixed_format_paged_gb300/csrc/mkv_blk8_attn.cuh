@@ -3,7 +3,9 @@
 // Mathematics.  For query row r of a kv head (rows: nq query tokens x G heads), token t of a page with scales
 // sk, sv and codes K_t, V_t (e4m3):
 //   s_rt = c sk (q_r . K_t),  c = softmax scale * log2(e);   out_r = sum_t 2^(s_rt - m_r) sv V_t / sum_t 2^(s_rt - m_r)
-// in one pass with running references (m for the sum, M for the weights 2^(s + log2 sv - M) of the codes).
+// in one pass with running references (m for the sum, M for the weights 2^(s + log2 sv - M) of the codes; M is kept as
+// M - m, and s - m is a difference of rounded scores, so that neither loses the page's scale nor the slack to the size
+// of the scores: ones of 1e30 still give their largest token's V).
 //
 // The codes are read as the first to leave L2, so that they do not push out what every CTA wants (the kernel's own
 // code, page ids, scales, the pieces for the join): 68.7 -> 65.2 us for 8 requests of 8K .. 32K tokens; with several
@@ -207,7 +209,7 @@ struct Cfg {
   static_assert(2 * kNS + kSub * kNP <= 512 && kCols * kCtas <= 512, "tensor memory");
   // fixed part of shared memory behind the slots
   static constexpr int kQ = 0, kP = kQ + 2 * kQBytes, kX = kP + 2 * kPBytes;         // x: [RT][128] floats
-  static constexpr int kRefs = kX + RT * 128 * 4;         // [2 pieces][WG][4][rows]: m, M, factors of l and O
+  static constexpr int kRefs = kX + RT * 128 * 4;         // [2 pieces][WG][4][rows]: m, M - m, factors of l and O
   static constexpr int kFac = kRefs + 2 * 4 * RT * 4;     // [2][RT] q factors, then [2][RT] visible limits
   static constexpr int kScale = kFac + 4 * RT * 4;        // [ring][8] k scale, [ring][8] log2 v scale
   static constexpr int kBars = kScale + kScaleRing * 16 * 4;
@@ -683,7 +685,7 @@ mkv_blk8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
           else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(part[k][0]);
         }
         if (lane == 0) {
-          qfac[(i & 1) * RT + r] = down * p.scale_log2;
+          qfac[(i & 1) * RT + r] = amax < INFINITY ? down * p.scale_log2 : NAN;   // (e4m3 has no infinity: its row is NaN)
           qlim[(i & 1) * RT + r] = have ? min(u.len, u.len - p.nq + qi + 1) : kv_end(p, u.len, u.rt, RT);
         }
       }
@@ -703,15 +705,15 @@ mkv_blk8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     for (int piece = -1; T > 0 && ok; ++piece) {          // (piece -1 has no tiles: it prepares the first)
       Unit nu{};
       int ncnt = 0;                                       // the next piece's tiles; 0 behind the last
-      float m[R], mv[R], l[R];
+      float m[R], md[R], l[R];                            // m, M - m, the sum
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        m[r] = mv[r] = kNone;
-        l[r] = 0.f;
+        m[r] = kNone;
+        md[r] = l[r] = 0.f;
       }
       // the references again, for the rolled loops (another buffer than the last piece's, which may still be read)
       float* const my_refs = refs + ((piece & 1) * C::kWG + wg) * 4 * R;
-      if (t < 2 * R) my_refs[t] = kNone;
+      if (t < 2 * R) my_refs[t] = t < R ? kNone : 0.f;
       int* const my_nan = nan_from + (C::kWG > 1 ? (piece & 1) * D : 0);    // (one warpgroup: a thread resets what it read)
       if (wg == 0)
         for (int d = t; d < D; d += 128) my_nan[d] = INT_MAX;
@@ -756,9 +758,8 @@ mkv_blk8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
           float most1 = -INFINITY, most2 = -INFINITY;
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            const float f = fac[r] * ks;
-            d1[r] = fmaf(a[r], f, -m[r]);
-            d2[r] = fmaf(a[r], f, lv - mv[r]);
+            d1[r] = __fmul_rn(a[r], fac[r] * ks) - m[r];  // (the score that m was taken from, not a more exact one)
+            d2[r] = d1[r] + (lv - md[r]);
           }
           if (hidden) {
 #pragma unroll
@@ -770,7 +771,7 @@ mkv_blk8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             most1 = fmaxf(most1, d1[r]);
             most2 = fmaxf(most2, d2[r]);
           }
-          if (raised) break;                              // (once: past 2^26 a score's own rounding exceeds the slack)
+          if (raised) break;
           const bool any = __any_sync(kFull, most1 > kRise || most2 > kRise + 4.f);
           int* const flag = my_flags + (votes & 1) * 4;
           if (lane == 0) flag[w4] = any;
@@ -779,27 +780,29 @@ mkv_blk8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
           if (!(f4.x | f4.y | f4.z | f4.w)) break;
           // raise the references: the scores to shared memory, a warp a row
 #pragma unroll
-          for (int r = 0; r < R; ++r) my_x[r * 128 + t] = hidden >> r & 1 ? -INFINITY : a[r] * (fac[r] * ks);
+          for (int r = 0; r < R; ++r) my_x[r * 128 + t] = hidden >> r & 1 ? -INFINITY : __fmul_rn(a[r], fac[r] * ks);
           if (!meet(b_red, reds)) break;
           const float lv4 = vscale[(j & (kScaleRing - 1)) * 8 + (4 * lane >> pshift)] - 4.f;    // of the page of tokens 4 lane ..
 #pragma unroll 1
           for (int r = w4; r < R; r += 4) {
             const float4 x = *reinterpret_cast<const float4*>(my_x + r * 128 + 4 * lane);
             const float top = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
-            const float om = my_refs[r], ov = my_refs[R + r];
-            const float nm = fmaxf(om, warp_max(top) + kRoom), nv = fmaxf(ov, warp_max(top + lv4) + kRoom);
+            const float om = my_refs[r], od = my_refs[R + r];
+            float nm = fmaxf(om, warp_max(top) + kRoom);
+            if (nm == INFINITY) nm = NAN;                 // a score that overflowed: its row is NaN from here on
+            const float nd = fmaxf(od + (om - nm), warp_max((top - nm) + lv4) + kRoom);
             if (lane == 0) {
               my_refs[r] = nm;
-              my_refs[R + r] = nv;
+              my_refs[R + r] = nd;
               my_refs[2 * R + r] = ex2(om - nm);
-              my_refs[3 * R + r] = ex2(ov - nv);
+              my_refs[3 * R + r] = ex2((om - nm) + (od - nd));
             }
           }
           if (!meet(b_red, reds)) break;
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             m[r] = my_refs[r];
-            mv[r] = my_refs[R + r];
+            md[r] = my_refs[R + r];
             l[r] *= my_refs[2 * R + r];
           }
           if (c > 0) {
@@ -890,9 +893,10 @@ mkv_blk8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             const int rr = r0 + r, row = u.rt * RT + row0 + rr;
             if (row >= p.rows) break;
             const float mr = my_refs[rr], L = my_refs[2 * R + rr];
-            const bool empty = L == 0.f;                    // no visible token
+            const bool empty = L == 0.f;                    // no token that counts; of a whole unit:
+            const bool lost = whole && empty && lim[rr] > 0;        // tokens, but all their scores fell below kNone
             // O holds 16 times the weights, relative to M
-            float f = ex2(my_refs[R + rr] - mr) * 0.0625f;
+            float f = ex2(my_refs[R + rr]) * 0.0625f;
             if (whole) f = f / L;
             float out[C::kSub];
 #pragma unroll
@@ -902,7 +906,7 @@ mkv_blk8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
 #pragma unroll
               for (int k = QP - 2; k >= 0; --k) out[d] = fmaf(out[d], 0.0625f, c4[2 * k]);
               out[d] = empty ? 0.f : out[d] * f;
-              if (lim[rr] > nan_at[d]) out[d] = NAN;
+              if (lim[rr] > nan_at[d] || lost) out[d] = NAN;
             }
             if (whole) {
               const int qi = p.by_G(row);
@@ -910,7 +914,7 @@ mkv_blk8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
 #pragma unroll
               for (int d = 0; d < C::kSub; ++d)
                 if (t < C::kW) store_out(p.out, p.q_f16, hrow * D + d * 128 + t, out[d]);
-              if (t == 0) p.lse[hrow] = empty ? -INFINITY : (mr + log2f(L)) * 0.69314718055994530942f;
+              if (t == 0) p.lse[hrow] = lost ? NAN : empty ? -INFINITY : (mr + log2f(L)) * 0.69314718055994530942f;
             } else {
               float* to = p.part + (static_cast<int64_t>(slot) * RT + row0 + rr) * (D + 4);
 #pragma unroll
@@ -1026,11 +1030,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) mkv_blk8_join_kernel(const __
   }
   __syncthreads();
   const bool empty = L == 0.f;
+  const float none = len - p.nq + static_cast<int>(qi) + 1 > 0 ? NAN : 0.f;      // (tokens, but no score above kNone; or no token)
 #pragma unroll
   for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps)
     store_out(p.out, p.q_f16, static_cast<int64_t>(hrow) * D + d,
-              empty ? 0.f : ((sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d])) / L);
-  if (threadIdx.x == 0) p.lse[hrow] = empty ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
+              empty ? none : ((sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d])) / L);
+  if (threadIdx.x == 0) p.lse[hrow] = empty ? (none == 0.f ? -INFINITY : none) : (M + log2f(L)) * 0.69314718055994530942f;
 }
 
 template <int D, int RT, int QP>
