@@ -638,14 +638,18 @@ mkv_status mkv_blk8_append(mkv_blk8* cache, int32_t layer, int32_t n, int32_t to
  * `dtype` (MKV_BF16 or MKV_F16), contiguous; lse: fp32 [n, nq, H_q] (natural log,
  * of scores times softmax_scale).  A query token that sees nothing (lens[b] <
  * nq - i) gets out 0 and lse -infinity.  Codes at positions past a sequence's
- * end are ignored, whatever they hold, and a NaN code reaches only the query tokens that see its token.  A
- * query row (token and head) with a NaN or an infinity that sees a token gets NaN, in out and lse, and so does
- * one with a score above fp32's range, or with none above -1e30 (in units of log 2).  Scores, sums and accumulators are fp32; q
- * enters exactly (elements below 2^-17 of their row's largest: to 2^-23 of it),
- * softmax weights with 8 significant bits (11 for MKV_F16), down to 2^-16 (2^-20)
- * of the largest weight so far times its page's scale.  The result does not
- * depend on anything but the inputs and the GPU's SM count.  Enqueued on
- * `stream`.  Errors: INVALID_ARGUMENT, CAPACITY (more than 2^31 tiles of 128
+ * end are ignored, whatever they hold, and a NaN code reaches only the query
+ * tokens that see its token.  A query row (token and head) with a NaN or an
+ * infinity that sees a token gets NaN, in out and lse, and so does one with a score
+ * above fp32's range, or with none above -1e30 (in units of log 2).  Scores, sums
+ * and accumulators are fp32; q enters exactly (elements below 2^-17 of their row's
+ * largest: to 2^-23 of it), softmax weights with 11 significant bits, 8 or more
+ * down to 2^-20 of the largest weight so far times its page's scale, and to
+ * within 2^-29 of that below, so that what small weights lose together stays
+ * below the output's rounding for a million tokens (bf16; fp16: a hundred
+ * thousand).  The result does not depend on anything but the inputs and the GPU's
+ * SM count.  Enqueued on `stream`.  Errors: INVALID_ARGUMENT, CAPACITY (more than
+ * 2^31 tiles of 128
  * tokens). */
 mkv_status mkv_blk8_attention(mkv_blk8* cache, int32_t layer, int32_t n, int32_t nq, const void* q, mkv_dtype dtype,
                               float softmax_scale, const int32_t* lens, const int32_t* table, int32_t table_width,

@@ -16,12 +16,19 @@
 // weights as N.  tcgen05.mma kind::f8f6f4 wants 8-bit operands on both sides, so q and the weights are split
 // into e4m3 parts that share N: a row q scaled by a power of two is q = q1 + q2 / 16 (+ q3 / 256), each part the
 // rounded remainder of the one before.  Four significant bits a part: two parts hold a bf16 q exactly and three an
-// fp16 one (up to its smallest elements: below 2^-17 of the row's largest a part is subnormal).  The weights take
-// as many, of their fp16 rounding: 8 bits for bf16 outputs, 11 for fp16 ones; the row sums use the unrounded fp32
-// weights.  P is the B operand with N contiguous (16-byte rows of one token), so that a thread stores its token's
-// weights in a few 16-byte words.
-// An N of 16 costs the tensor pipe what N = 8 does, and no code is ever converted, so the ALUs see only the
-// scores: nothing in the kernel scales with head_dim but the copies and the MMAs.
+// fp16 one (up to its smallest elements: below 2^-17 of the row's largest a part is subnormal).
+// The weights (times 2^6, of their fp16 rounding) take four parts, of steps 1, 2^-4, 2^-11 and 2^-15.  What matters is
+// not how many bits a weight has but what all of them miss together: a long context behind one dominant token is
+// a hundred thousand weights of 2^-17, whose sum counts as much as that token, and parts of steps 1 and 2^-4 alone
+// round every one of them to the same wrong value (65,536 tokens 11 nats below the first: outputs 23 to 56 % off).  The
+// first two parts hold the 8 leading bits of weights above 2^-10 of the reference and the last two, 2^7 further down,
+// their remainder (11 bits in all) and the leading bits of the weights below: 2^-8 or better down to 2^-22 of the
+// reference, and an error of 2^-31 of it for what is smaller still, against a largest weight of 2^-2 or more: a million
+// tokens lose 2^-9 together.  The row sums use the unrounded fp32 weights.
+// P is the B operand with N contiguous (16-byte groups of one token), so that a thread stores its token's weights in
+// two 16-byte words.
+// An N of 32 costs the tensor pipe what N = 8 does (reading A bounds it), and no code is ever converted, so the ALUs see
+// only the scores: nothing in the kernel scales with head_dim but the copies and the MMAs.
 //
 // Bound: memory, 2 D bytes a token and kv head.  Work is cut into tiles of 128 tokens of one (sequence, kv head,
 // row tile); every CTA takes the same number of tiles, one after another, whatever sequences they belong to (the
@@ -34,8 +41,8 @@
 // 8 x 8K .. 32K tokens with 24 rows, head_dim 256, fp16; 42 against 37 for 6 x 4K .. 18K with 30 rows, head_dim 64:
 // a tile's softmax is a chain of short dependent steps, and more warps hide them.)  S is double-buffered: the next
 // tile's QK runs while this tile's softmax does.  The maximum is looked at by one vote a tile (does any
-// score exceed its reference by 2^4?) and reduced only then, to a reference 2^2 above it, which is rare after the
-// first tile of a piece; weights therefore lie in [0, 16] and their first parts, scaled by 16, in e4m3's range.
+// score exceed its reference by 2^2?) and reduced only then, to a reference 2^2 above it, which is rare after the
+// first tile of a piece; weights therefore lie in [0, 4] and their first parts, scaled by 2^6, in e4m3's range.
 // What is not done every tile (the references, a piece's end, the producer's start) is written as rolled loops over rows
 // kept in shared memory: a launch meets its instructions cold, about 80 cycles per 128 bytes of code, and unrolled those
 // paths cost 7,000 cycles the first time against a tile's 2,600.  For the same reason nothing is divided where a product
@@ -68,9 +75,12 @@ namespace b8 {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr long long kWaitCycles = 4000000000LL;   // ~2 s: bound on any wait
-constexpr float kRise = 4.0f;                      // log2 units a score may exceed its reference by
+constexpr float kRise = 2.0f;                      // log2 units a score may exceed its reference by
 constexpr float kRoom = 2.0f;                      // and that a raised reference lies above the largest score
 constexpr float kNone = -1e30f;                    // reference before any visible token
+constexpr float kUp = 6.0f;                        // log2 of the factor that weights carry into their parts
+constexpr int kWP = 4;                             // parts of a weight
+constexpr __host__ __device__ float part_step(int k) { return k == 2 ? 128.f : 16.f; }   // step of part k - 1 over part k's
 constexpr int kScaleRing = 8;                      // tiles whose page scales are kept
 
 // ------------------------------------------------------------------ PTX
@@ -197,7 +207,7 @@ struct Cfg {
   static constexpr int kNS = round16(QP * RT);            // columns of S
   static constexpr int kWG = RT / 8;            // softmax warpgroups
   static constexpr int kRows = RT / kWG;                  // rows of one
-  static constexpr int kPG = round16(QP * kRows) / 16;    // 16-byte groups of a warpgroup's weights
+  static constexpr int kPG = kWP * kRows / 16;            // 16-byte groups of a warpgroup's weights
   static constexpr int kNP = 16 * kPG * kWG;              // columns of O
   static constexpr int kSoft = 128 * kWG, kThreads = kSoft + 64;
   static_assert(kRows % 4 == 0, "rows of a warpgroup");
@@ -544,7 +554,7 @@ mkv_blk8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
           if (!issue(&kmap, id, z)) break;
           if (lane < ppt) {
             kscale[(j & (kScaleRing - 1)) * 8 + lane] = ks;
-            vscale[(j & (kScaleRing - 1)) * 8 + lane] = __log2f(vs) + 4.f;    // with the factor 16 of the first part
+            vscale[(j & (kScaleRing - 1)) * 8 + lane] = __log2f(vs) + kUp;
           }
           release();
           if (j > 0) {
@@ -772,7 +782,7 @@ mkv_blk8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             most2 = fmaxf(most2, d2[r]);
           }
           if (raised) break;
-          const bool any = __any_sync(kFull, most1 > kRise || most2 > kRise + 4.f);
+          const bool any = __any_sync(kFull, most1 > kRise || most2 > kRise + kUp);
           int* const flag = my_flags + (votes & 1) * 4;
           if (lane == 0) flag[w4] = any;
           if (!meet(b_vote, votes)) break;
@@ -782,7 +792,7 @@ mkv_blk8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
 #pragma unroll
           for (int r = 0; r < R; ++r) my_x[r * 128 + t] = hidden >> r & 1 ? -INFINITY : __fmul_rn(a[r], fac[r] * ks);
           if (!meet(b_red, reds)) break;
-          const float lv4 = vscale[(j & (kScaleRing - 1)) * 8 + (4 * lane >> pshift)] - 4.f;    // of the page of tokens 4 lane ..
+          const float lv4 = vscale[(j & (kScaleRing - 1)) * 8 + (4 * lane >> pshift)] - kUp;    // of the page of tokens 4 lane ..
 #pragma unroll 1
           for (int r = w4; r < R; r += 4) {
             const float4 x = *reinterpret_cast<const float4*>(my_x + r * 128 + 4 * lane);
@@ -811,21 +821,21 @@ mkv_blk8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
 #pragma unroll 1
             for (int i = 0; i < R / 4 * C::kSub; ++i) {   // four rows of O, 128 dims
               const int r0 = i / C::kSub * 4, d = i % C::kSub;
-              const uint32_t at = tmem + lanes + C::kTO + d * C::kNP + wg * C::kPG * 16 + QP * r0;
+              const uint32_t at = tmem + lanes + C::kTO + d * C::kNP + wg * C::kPG * 16 + kWP * r0;
               const float4 fo = *reinterpret_cast<const float4*>(my_refs + 3 * R + r0);
-              float o[4 * QP];
-              tm_ld<4 * QP>(at, o);
+              float o[4 * kWP];
+              tm_ld<4 * kWP>(at, o);
               tm_wait_ld(o);
 #pragma unroll
-              for (int k = 0; k < 4 * QP; ++k)
-                o[k] *= k / (2 * QP) ? (k % 2 ? fo.w : fo.z) : (k % 2 ? fo.y : fo.x);
-              tm_st<4 * QP>(at, o);
+              for (int k = 0; k < 4 * kWP; ++k)
+                o[k] *= k / (2 * kWP) ? (k % 2 ? fo.w : fo.z) : (k % 2 ? fo.y : fo.x);
+              tm_st<4 * kWP>(at, o);
             }
             tm_wait_st();
           }
         }
         if (!ok) break;
-        // weights: byte n = QP (r - r % 2) + 2 part + r % 2 of this token's row, 16 bytes a group
+        // weights: byte n = kWP (r - r % 2) + 2 part + r % 2 of this token's row, 16 bytes a group
         uint32_t words[4 * C::kPG];
 #pragma unroll
         for (int i = 0; i < 4 * C::kPG; ++i) words[i] = 0;
@@ -835,11 +845,11 @@ mkv_blk8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
           l[r + 1] += ex2(d1[r + 1]);
           __half2 w = __floats2half2_rn(ex2(d2[r]), ex2(d2[r + 1]));
 #pragma unroll
-          for (int k = 0; k < QP; ++k) {
-            const int hw = QP * r / 2 + k;
+          for (int k = 0; k < kWP; ++k) {                 // (a remainder past e4m3's range is cut to it: it only errs less)
+            const int hw = kWP * r / 2 + k;
             const uint32_t two = e4m3x2(w);
             words[hw / 2] |= two << (16 * (hw % 2));
-            if (k + 1 < QP) w = __hmul2(__hsub2(w, half2_of(two)), __float2half2_rn(16.f));
+            if (k + 1 < kWP) w = __hmul2(__hsub2(w, half2_of(two)), __float2half2_rn(part_step(k + 1)));
           }
         }
 #pragma unroll
@@ -883,9 +893,9 @@ mkv_blk8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         for (int d = 0; d < C::kSub; ++d) nan_at[d] = my_nan[d * 128 + min(t, C::kW - 1)];
 #pragma unroll 1
         for (int r0 = 0; r0 < R && u.rt * RT + row0 + r0 < p.rows; r0 += 4) {
-          float o[C::kSub][4 * QP];
+          float o[C::kSub][4 * kWP];
 #pragma unroll
-          for (int d = 0; d < C::kSub; ++d) tm_ld<4 * QP>(tmem + lanes + C::kTO + d * C::kNP + wg * C::kPG * 16 + QP * r0, o[d]);
+          for (int d = 0; d < C::kSub; ++d) tm_ld<4 * kWP>(tmem + lanes + C::kTO + d * C::kNP + wg * C::kPG * 16 + kWP * r0, o[d]);
 #pragma unroll
           for (int d = 0; d < C::kSub; ++d) tm_wait_ld(o[d]);
 #pragma unroll
@@ -895,16 +905,16 @@ mkv_blk8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             const float mr = my_refs[rr], L = my_refs[2 * R + rr];
             const bool empty = L == 0.f;                    // no token that counts; of a whole unit:
             const bool lost = whole && empty && lim[rr] > 0;        // tokens, but all their scores fell below kNone
-            // O holds 16 times the weights, relative to M
-            float f = ex2(my_refs[R + rr]) * 0.0625f;
+            // O holds 2^kUp times the weights, relative to M
+            float f = ex2(my_refs[R + rr] - kUp);
             if (whole) f = f / L;
             float out[C::kSub];
 #pragma unroll
             for (int d = 0; d < C::kSub; ++d) {
-              const float* c4 = o[d] + r / 2 * 2 * QP + r % 2;      // the row's parts lie two columns apart
-              out[d] = c4[2 * (QP - 1)];
+              const float* c4 = o[d] + r / 2 * 2 * kWP + r % 2;     // the row's parts lie two columns apart
+              out[d] = c4[2 * (kWP - 1)];
 #pragma unroll
-              for (int k = QP - 2; k >= 0; --k) out[d] = fmaf(out[d], 0.0625f, c4[2 * k]);
+              for (int k = kWP - 2; k >= 0; --k) out[d] = fmaf(out[d], 1.f / part_step(k + 1), c4[2 * k]);
               out[d] = empty ? 0.f : out[d] * f;
               if (lim[rr] > nan_at[d] || lost) out[d] = NAN;
             }
