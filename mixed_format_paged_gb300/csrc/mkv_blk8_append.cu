@@ -218,26 +218,31 @@ mkv_blk8_append_kernel(const __grid_constant__ B8AppendParams p) {
       reinterpret_cast<uint2*>(codes)[u] = w;
     }
   }
+  auto put = [&](int j, const float (&y)[8]) {
+    uint2 w;
+    w.x = e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16);
+    w.y = e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16);
+    reinterpret_cast<uint2*>(codes)[(t0 << shift) + threadIdx.x + j * THREADS] = w;
+  };
+  if (inf || odd) {                                     // (apart: among the values of every page, 37.0 us became 38.8)
+#pragma unroll 1
+    for (int j = 0; j * rows < work; ++j) {
+      float y[8];
+      get8(stage + j * THREADS * 8, y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = !finite(y[i]) ? NAN : odd ? __fdiv_rn(y[i], now) : y[i] * inv;
+      put(j, y);
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     if (j * rows >= work) break;
     float y[8];
     get8(stage + j * THREADS * 8, y);
-    if (inf) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = finite(y[i]) ? y[i] : NAN;
-    }
-    if (odd) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(y[i], now);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] *= inv;
-    }
-    uint2 w;
-    w.x = e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16);
-    w.y = e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16);
-    reinterpret_cast<uint2*>(codes)[(t0 << shift) + threadIdx.x + j * THREADS] = w;
+    for (int i = 0; i < 8; ++i) y[i] *= inv;
+    put(j, y);
   }
 }
 
