@@ -5,7 +5,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
-from .rope import current_stream
+from .rope import current_stream, outputs
 
 _I32 = torch.int32
 _DTYPES = {torch.float32: B.MKV_F32, torch.bfloat16: B.MKV_BF16, torch.float16: B.MKV_F16}
@@ -115,11 +115,11 @@ class Blk8Cache:
         shape = (n, nq, self.num_q_heads, self.head_dim)
         self._check(q, "q", shape, (torch.bfloat16, torch.float16))
         if out is None:
-            out = torch.empty_like(q)
+            out, = outputs(stream, q.device, lambda: torch.empty_like(q))
         else:
             self._check(out, "out", shape, (q.dtype,))
         if lse is None:
-            lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
+            lse, = outputs(stream, q.device, lambda: torch.empty(shape[:3], dtype=torch.float32, device=q.device))
         else:
             self._check(lse, "lse", shape[:3], (torch.float32,))
         scale = self.head_dim ** -0.5 if scale is None else scale

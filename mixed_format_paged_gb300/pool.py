@@ -5,7 +5,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
-from .rope import Rope, current_stream
+from .rope import Rope, current_stream, outputs
 
 
 class MkvPool:
@@ -48,6 +48,10 @@ class MkvPool:
             return current_stream(self.device_index)
         return stream
 
+    @staticmethod
+    def _new(stream, shape, device, dtype=torch.float32, make=torch.empty):
+        return outputs(stream, device, lambda: make(shape, dtype=dtype, device=device))[0]
+
     # ------------------------------------------------------------- forwarding
     def extend(self, seq_ids, n_new):
         B.mkv_seq_extend(self.handle, seq_ids, n_new)
@@ -79,7 +83,7 @@ class MkvPool:
         if q is None and q_out is not None:
             raise ValueError("q_out without q")
         if q is not None and q_out is None:
-            q_out = torch.empty_like(q)
+            q_out, = outputs(stream, q.device, lambda: torch.empty_like(q))
         dtype, kv = k.dtype, (T, self.num_kv_heads, d)
         if dtype is not torch.bfloat16 and dtype is not torch.float32:
             raise TypeError("q, k and v must all be float32 or all be bfloat16")
@@ -121,9 +125,9 @@ class MkvPool:
         if q.dtype not in (torch.bfloat16, torch.float32) or not q.is_contiguous():
             raise TypeError("q must be a contiguous float32 or bfloat16 tensor")
         if out is None:
-            out = torch.empty((n, self.num_q_heads, self.head_dim), dtype=torch.float32, device=q.device)
+            out = self._new(stream, (n, self.num_q_heads, self.head_dim), q.device)
         if lse is None:
-            lse = torch.empty((n, self.num_q_heads), dtype=torch.float32, device=q.device)
+            lse = self._new(stream, (n, self.num_q_heads), q.device)
         dtype = B.MKV_BF16 if q.dtype == torch.bfloat16 else B.MKV_F32
         B.mkv_decode_attention(self.handle, layer, seq_ids, q, dtype, out, lse, self._stream(stream))
         return out, lse
@@ -137,9 +141,9 @@ class MkvPool:
         if q.dtype not in (torch.bfloat16, torch.float32) or not q.is_contiguous() or q.dim() != 4:
             raise TypeError("q must be a contiguous [n, nq, H_q, d] float32 or bfloat16 tensor")
         if out is None:
-            out = torch.empty((n, nq, self.num_q_heads, self.head_dim), dtype=torch.float32, device=q.device)
+            out = self._new(stream, (n, nq, self.num_q_heads, self.head_dim), q.device)
         if lse is None:
-            lse = torch.empty((n, nq, self.num_q_heads), dtype=torch.float32, device=q.device)
+            lse = self._new(stream, (n, nq, self.num_q_heads), q.device)
         dtype = B.MKV_BF16 if q.dtype == torch.bfloat16 else B.MKV_F32
         B.mkv_decode_attention_multi(self.handle, layer, seq_ids, nq, q, dtype, out, lse, self._stream(stream))
         return out, lse
@@ -149,9 +153,9 @@ class MkvPool:
         """Append each sequence's newest token (k, v: [n, H_kv, d]) and decode (q: [n, H_q, d])."""
         n = len(seq_ids)
         if out is None:
-            out = torch.empty((n, self.num_q_heads, self.head_dim), dtype=torch.float32, device=q.device)
+            out = self._new(stream, (n, self.num_q_heads, self.head_dim), q.device)
         if lse is None:
-            lse = torch.empty((n, self.num_q_heads), dtype=torch.float32, device=q.device)
+            lse = self._new(stream, (n, self.num_q_heads), q.device)
         kvd = B.MKV_BF16 if k.dtype == torch.bfloat16 else B.MKV_F32
         qd = B.MKV_BF16 if q.dtype == torch.bfloat16 else B.MKV_F32
         B.mkv_append_decode(self.handle, layer, seq_ids, k, v, kvd, q, qd, out, lse, self._stream(stream))
@@ -162,7 +166,7 @@ class MkvPool:
         pages) of the decode query q with that call's lse (mkv_page_relevance)."""
         n = len(seq_ids)
         npg = max(self.seq_info(r)[1] for r in seq_ids)
-        mass = torch.zeros((n, npg), dtype=torch.float32, device=q.device)
+        mass = self._new(stream, (n, npg), q.device, make=torch.zeros)
         qd = B.MKV_BF16 if q.dtype == torch.bfloat16 else B.MKV_F32
         B.mkv_page_relevance(self.handle, layer, seq_ids, q, qd, lse, mass, npg, self._stream(stream))
         return mass
@@ -179,8 +183,8 @@ class MkvPool:
     def dequantize(self, layer: int, seq: int, page0: int, npages: int, dtype=torch.float32, stream=None):
         """Dense K, V [npages * P, H_kv, d] of pages [page0, page0 + npages)."""
         shape = (npages * self.page_size, self.num_kv_heads, self.head_dim)
-        k = torch.empty(shape, dtype=dtype, device=self.buf.device)
-        v = torch.empty(shape, dtype=dtype, device=self.buf.device)
+        k = self._new(stream, shape, self.buf.device, dtype)
+        v = self._new(stream, shape, self.buf.device, dtype)
         od = B.MKV_BF16 if dtype == torch.bfloat16 else B.MKV_F32
         B.mkv_dequantize_pages(self.handle, layer, seq, page0, npages, k, v, od, self._stream(stream))
         return k, v

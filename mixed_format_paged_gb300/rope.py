@@ -16,6 +16,23 @@ def current_stream(index: int) -> int:
     return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
 
 
+def outputs(stream, device: torch.device, *make):
+    """New tensors make[i]() for a call on `stream` (None: the current one, which costs nothing more).  Where that is
+    another one, their memory is `stream`'s, so that no earlier tensor's work on the current stream still uses it, and
+    it is not given away, once they are freed, before the current stream is through with them."""
+    if stream is not None and device.type == "cuda":
+        raw = stream if isinstance(stream, int) else stream.cuda_stream
+        current = torch.cuda.current_stream(device)
+        if raw != current.cuda_stream:
+            on = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+            with torch.cuda.stream(on):
+                new = [f() for f in make]
+            for x in new:
+                x.record_stream(current)
+            return new
+    return [f() for f in make]
+
+
 class Rope:
     """Rotary positions of the first `rot_dim` dims of a head; ``scaling`` is
     "none", "linear", "ntk", "yarn" or "wavelength" (see mkv_rope_scaling).
@@ -43,7 +60,7 @@ class Rope:
         return self.table.mscale
 
     @staticmethod
-    def _rows(name, x, out, tokens, d, like):
+    def _rows(name, x, out, tokens, d, like, stream):
         """(output, C arguments) of q or k; out None: a new contiguous tensor."""
         shape, st = x.shape, x.stride()
         if len(shape) != 3 or shape[0] != tokens or shape[2] != d or (d > 1 and st[2] != 1):
@@ -52,7 +69,8 @@ class Rope:
             raise TypeError("q, k and their outputs must share one dtype and device")
         heads = shape[1]
         if out is None:
-            out = torch.empty_like(x, memory_format=torch.contiguous_format)
+            new = lambda: torch.empty_like(x, memory_format=torch.contiguous_format)  # noqa: E731
+            out = new() if stream is None else outputs(stream, x.device, new)[0]
             return out, B.RopeRows(x.data_ptr(), out.data_ptr(), heads, 0, st[0], st[1], heads * d, d)
         so = out.stride()
         if out.shape != shape or (d > 1 and so[2] != 1):
@@ -77,10 +95,10 @@ class Rope:
             raise TypeError("positions must be a contiguous [T] int32 or int64 tensor")
         if positions.device != device or device.type != "cuda":
             raise TypeError("q and positions must be on one CUDA device")
-        q_out, rows_q = self._rows("q", q, q_out, T, d, q)
+        q_out, rows_q = self._rows("q", q, q_out, T, d, q, stream)
         rows_k = None
         if k is not None:
-            k_out, rows_k = self._rows("k", k, k_out, T, d, q)
+            k_out, rows_k = self._rows("k", k, k_out, T, d, q, stream)
         if stream is None:
             stream = current_stream(device.index)
         args = (self.table, T, d, positions, 8 if pt is torch.int64 else 4, rows_q, rows_k, dtype, inverse, stream)
