@@ -85,10 +85,15 @@ class Rope:
         """Rotate q [T, Hq, d] and k [T, Hkv, d] (or None) at positions [T] (int32
         or int64, on the device).  Returns (q_out, k_out); pass q_out=q, k_out=k
         to work in place.  inverse: the transpose, i.e. the gradients of q and k
-        from those of the outputs."""
+        from those of the outputs.  The call is not recorded by autograd, and
+        refuses tensors that it would have to be recorded for."""
         dtype = _DTYPES.get(q.dtype)
         if dtype is None:
             raise TypeError("q must be float32, bfloat16 or float16")
+        if torch.is_grad_enabled() and (q.requires_grad or k is not None and k.requires_grad or
+                                        q_out is not None and q_out.requires_grad or k_out is not None and k_out.requires_grad):
+            raise RuntimeError("Rope is not recorded by autograd: call it under torch.no_grad() (an autograd function's "
+                               "forward is), with inverse=True for the gradients")
         T, d, device = q.shape[0], q.shape[-1], q.device
         pt = positions.dtype
         if (pt is not torch.int64 and pt is not torch.int32) or positions.shape != (T,) or not positions.is_contiguous():

@@ -108,6 +108,42 @@ def test_bad_table_arguments_in_python(mkv):
         mkv.Rope(8, inv_freq=[1.0])
 
 
+def test_tensors_that_autograd_would_record_are_refused(mkv):
+    rope, pos = mkv.Rope(16), torch.zeros(3, dtype=torch.int64)
+    x, w = torch.zeros(3, 2, 16), torch.zeros(3, 2, 16, requires_grad=True)
+    for args, kw in (((w, None, pos), {}), ((x, w, pos), {}), ((w * 2, x, pos), {}), ((x, x, pos), dict(q_out=w)),
+                     ((x, x, pos), dict(k_out=w)), ((w, w, pos), dict(inverse=True))):
+        with pytest.raises(RuntimeError, match="autograd"):
+            rope(*args, **kw)
+        with torch.no_grad(), pytest.raises(TypeError, match="CUDA"):        # past that check, to the next (no device here)
+            rope(*args, **kw)
+    with pytest.raises(TypeError, match="CUDA"):
+        rope(x, x, pos)
+
+
+@pytest.mark.gpu
+def test_rope_inside_an_autograd_function_has_the_formulas_gradient(mkv):
+    rope = mkv.Rope(32, interleaved=True)
+
+    class Rotate(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, pos):
+            ctx.save_for_backward(pos)
+            return rope(x, None, pos)[0]
+
+        @staticmethod
+        def backward(ctx, grad):
+            return rope(grad.contiguous(), None, ctx.saved_tensors[0], inverse=True)[0], None
+
+    g = torch.Generator().manual_seed(1)
+    pos = torch.arange(9).to(DEV)
+    x = torch.randn(9, 3, 48, generator=g).to(DEV).requires_grad_()
+    up = torch.randn(9, 3, 48, generator=g).to(DEV)
+    Rotate.apply(x, pos).backward(up)
+    ref, size = _reference(up.double().cpu().numpy(), pos.cpu().numpy(), rope.inv_freq, rope.mscale, True, transpose=True)
+    _close(x.grad, ref, size, pos.cpu().numpy(), rope.inv_freq, torch.float32)
+
+
 def _rows(mkv, heads=2, d=16, ptr=0x1000, out=0x100000, **kw):
     a = dict(inp=ptr, out=out, heads=heads, reserved=0, in_token=heads * d, in_head=d, out_token=heads * d, out_head=d)
     a.update(kw)
