@@ -199,8 +199,8 @@ mkv_status mkv_seq_release(mkv_pool* pool, int32_t seq);
  * appear several times: parallel samples, beams).  Full pages are shared and
  * cost nothing; a partial tail page (always FP8) is copied into a fresh FP8
  * slot, only the rows of its tokens, in every layer, on `stream`.  Afterwards
- * the sequences are independent: each extends, demotes (into a TQ3 page of its
- * own) and releases by itself, and a slot is freed when its last sequence lets
+ * the sequences are independent: each extends, demotes (see mkv_demote_pages) and
+ * releases by itself, and a slot is freed when its last sequence lets
  * go of it.  A page that is shared is read only: mkv_append_tokens,
  * mkv_append_rope, mkv_append_decode and the step graph refuse to write one
  * (INVALID_STATE), which only a caller meets that forks between mkv_seq_extend
@@ -346,8 +346,9 @@ mkv_status mkv_set_tier(mkv_pool* pool, int32_t seq, int32_t page, mkv_tier tier
 /* FP8 -> TQ3 demotion ("older non-anchor pages move to packed TQ3",
  * abstract): for each (seq_ids[i], pages[i]), re-encode the page of every
  * layer as "TQ3 row" above into a fresh TQ3 slot, tag it STALE and free its
- * FP8 slot (stream-ordered reuse; a shared page stays for the others).
- * All-or-nothing checks first:
+ * FP8 slot (stream-ordered reuse).  Of a page that forked sequences share, those
+ * of the call share one TQ3 page and the others keep the FP8 one: demote it for
+ * all of them in one call, or each call adds a copy.  All-or-nothing checks first:
  * INVALID_STATE for an Anchor page, a TQ3 page, a partial (not full) page or
  * a page listed twice; OUT_OF_PAGES when the TQ3 arena is short. */
 mkv_status mkv_demote_pages(mkv_pool* pool, int32_t n, const int32_t* seq_ids, const int32_t* pages,

@@ -1353,14 +1353,23 @@ mkv_status mkv_demote_pages(mkv_pool* p, int32_t n, const int32_t* ids, const in
   std::sort(seen.begin(), seen.end());
   for (size_t i = 1; i < seen.size(); ++i)
     if (seen[i] == seen[i - 1]) return fail(MKV_ERR_INVALID_STATE, "page listed twice");
-  if (int64_t(n) > int64_t(p->free_tq3.size()))
-    return fail(MKV_ERR_OUT_OF_PAGES, "TQ3 arena: need %d free slots, have %zu", n, p->free_tq3.size());
-  if (n == 0) return MKV_OK;
-  std::vector<int2> pairs(n);
+  // a page that sequences of the call share stays shared: one TQ3 slot for it
+  std::vector<int2> pairs;
+  std::vector<int32_t> to(static_cast<size_t>(n));        // TQ3 slots, as places in `pairs` first
+  std::unordered_map<int32_t, int32_t> at;
+  pairs.reserve(size_t(n));
   for (int i = 0; i < n; ++i) {
-    pairs[i].x = p->seqs[ids[i]].pages[pages[i]].slot;
-    pairs[i].y = p->free_tq3[p->free_tq3.size() - 1 - i];
+    const int32_t slot = p->seqs[ids[i]].pages[pages[i]].slot;
+    to[i] = int32_t(pairs.size());
+    if (p->ref_fp8[slot] > 1) to[i] = at.try_emplace(slot, to[i]).first->second;
+    if (to[i] == int32_t(pairs.size())) pairs.push_back({slot, 0});
   }
+  const int npairs = int(pairs.size());
+  if (pairs.size() > p->free_tq3.size())
+    return fail(MKV_ERR_OUT_OF_PAGES, "TQ3 arena: need %d free slots, have %zu", npairs, p->free_tq3.size());
+  if (n == 0) return MKV_OK;
+  for (int i = 0; i < npairs; ++i) pairs[i].y = p->free_tq3[p->free_tq3.size() - 1 - i];
+  for (int32_t& x : to) x = pairs[x].y;
   if (!p->host_only) {
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     DemoteParams dp{};
@@ -1375,8 +1384,8 @@ mkv_status mkv_demote_pages(mkv_pool* p, int32_t n, const int32_t* ids, const in
     dp.P = P;
     std::memcpy(dp.signs, p->signs, sizeof dp.signs);
     std::memcpy(dp.thr, codebook().thr, sizeof dp.thr);
-    for (int i0 = 0; i0 < n; i0 += p->demote_cap) {
-      const int cnt = std::min(p->demote_cap, n - i0);
+    for (int i0 = 0; i0 < npairs; i0 += p->demote_cap) {
+      const int cnt = std::min(p->demote_cap, npairs - i0);
       mkv_status st = staging_acquire(p->st_demote);
       if (st != MKV_OK) return st;
       std::memcpy(p->st_demote.host, pairs.data() + i0, size_t(cnt) * sizeof(int2));
@@ -1390,11 +1399,11 @@ mkv_status mkv_demote_pages(mkv_pool* p, int32_t n, const int32_t* ids, const in
   for (int i = 0; i < n; ++i) {
     PageRec& r = p->seqs[ids[i]].pages[pages[i]];
     drop_ref(p, false, r.slot);
-    r.slot = pairs[i].y;
+    r.slot = to[i];
     r.tier = int8_t(MKV_TIER_STALE);
-    p->ref_tq3[r.slot] = 1;
+    ++p->ref_tq3[r.slot];
   }
-  p->free_tq3.resize(p->free_tq3.size() - n);
+  p->free_tq3.resize(p->free_tq3.size() - size_t(npairs));
   ++p->generation;
   return MKV_OK;
 }

@@ -554,3 +554,46 @@ def test_appends_of_iterators_write_what_lists_write(mkv):
         got.append([out] + [x for layer in range(2) for r in range(2) for x in _dense(pool, layer, r)])
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ demotions of shared pages
+def test_a_demotion_of_all_owners_keeps_a_page_shared(mkv):
+    p = _host(mkv, tq3_slots=2)
+    p.extend([0], [64 * 3 + 1])
+    p.fork([0, 0, 0], [1, 2, 3])
+    free = p.stats().fp8_slots_free
+    before = p.stats().fp8_bytes + p.stats().tq3_bytes
+    p.demote([0, 1, 2, 3, 1, 0], [0, 0, 0, 0, 2, 2])     # page 2 for two of its owners
+    assert len({_slots(p, r)[0] for r in range(4)}) == 1 and _slots(p, 0)[0][0] == 3
+    assert _slots(p, 0)[2] == _slots(p, 1)[2] != _slots(p, 2)[2] == _slots(p, 3)[2]
+    st = p.stats()
+    assert st.tq3_slots_free == 0 and st.fp8_slots_free == free + 1
+    assert st.fp8_bytes + st.tq3_bytes == before - 2 * 132096 + 2 * 2 * 50176
+    _refused(mkv, 3, p.demote, [2, 3], [2, 2])           # one more slot is needed, and nothing changes
+    assert _slots(p, 2)[2][0] == 1
+    for r in (1, 3, 0, 2):
+        p.release(r)
+    st = p.stats()
+    assert st.tq3_slots_free == 2 and st.fp8_slots_free == 12
+
+
+@pytest.mark.gpu
+def test_a_shared_demoted_page_holds_what_an_unshared_one_does(mkv):
+    pool, g = _fill(mkv, lens=(5 * 64 + 17, 130))
+    alone, _ = _fill(mkv, lens=(5 * 64 + 17, 130))
+    for x in (pool, alone):
+        x.fork([0, 1, 0], [2, 3, 4])
+    pages = [([0, 2, 4, 1, 3], [1, 1, 1, 0, 0]), ([0, 2, 4], [3, 3, 3])]
+    for ids, pgs in pages:
+        pool.demote(ids, pgs)
+        for r, pg in zip(ids, pgs):                       # one by one: a copy each
+            alone.demote([r], [pg])
+    assert pool.stats().tq3_slots_free == 20 - 3 and alone.stats().tq3_slots_free == 20 - 8
+    q = torch.randn(5, 24, 256, generator=g).to(DEV)
+    for layer in range(3):
+        for r in range(5):
+            for a, b in zip(_dense(pool, layer, r), _dense(alone, layer, r)):
+                assert torch.equal(a, b)
+        for a, b in zip(pool.decode(layer, range(5), q), alone.decode(layer, range(5), q)):     # the same plan
+            assert torch.equal(a, b)
+    pool.check_device_errors()
