@@ -212,7 +212,7 @@ mkv_status mkv_seq_fork(mkv_pool* pool, int32_t n, const int32_t* src_ids, const
 
 /* Cut sequences back to new_len[i] <= length tokens (rejected speculative
  * tokens, a dropped beam; 0 empties it): pages past the end return to the free
- * lists.  A page that becomes partial must be FP8 (INVALID_STATE for TQ3); if
+ * lists, and what the cut rows held, NaNs too, reaches no later result.  A page that becomes partial must be FP8 (INVALID_STATE for TQ3); if
  * it is shared, its remaining rows are copied into a fresh FP8 slot on `stream`.
  * All-or-nothing: INVALID_ARGUMENT (ids, an id listed twice, lengths),
  * OUT_OF_PAGES (a free slot per such shared page; the pages that the call

@@ -2,8 +2,8 @@
 //
 // Bound: memory, twice the bytes of the rows that hold tokens.  One block per (page, layer, kv head) copies
 // its K and V planes; of a page that is not full, only the rows of its tokens (a V token pair is one
-// 2 d-byte run, so an odd count rounds up) and their scales.  The rows past them keep what the slot held:
-// every stored byte of an FP8 arena is a finite code and the attention kernels give those rows weight 0.
+// 2 d-byte run, so an odd count rounds up) and their scales.  The rows past them keep what the slot held, which
+// the attention kernels clear on their way.
 // The list of pages travels as a kernel parameter: no upload, no buffer that a later call could overwrite.
 // Measured (HBM copy rate 6,695 GB/s): 64 tail pages of 16 layers x 4 kv heads, 135 MB, 22.2 us with its launch (91 %);
 // 8 sequences whole, 1.25 GB, 180.5 us (104 %: the rate is a copy of another length).

@@ -597,3 +597,53 @@ def test_a_shared_demoted_page_holds_what_an_unshared_one_does(mkv):
         for a, b in zip(pool.decode(layer, range(5), q), alone.decode(layer, range(5), q)):     # the same plan
             assert torch.equal(a, b)
     pool.check_device_errors()
+
+
+# ------------------------------------------------------------------ what lies behind a sequence's end
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+@pytest.mark.parametrize("P,keep", [(64, 66), (64, 65), (128, 143), (64, 3)])
+def test_rows_behind_the_end_of_a_sequence_reach_nobody(mkv, P, keep, bad):
+    """Rows with NaNs and infinities are cut off (or their sequence is released): the shorter sequence, its fork, and the
+    next one in the freed pages decode as they do in a pool that never held such rows."""
+    H, D, n = 4, 256, keep + 7
+    g = torch.Generator().manual_seed(keep)
+    k, v = (torch.randn(n, H, D, generator=g).to(DEV) for _ in range(2))
+    kb, vb = k.clone(), v.clone()
+    for x in (kb, vb):
+        x[keep:, :, 11] = float(bad)
+        x[keep + 1:, :, 200] = -float(bad)
+    pools = []
+    for rows in ((k, v), (kb, vb)):
+        pool = mkv.MkvPool(1, 24, H, D, P, 8, 2, max_seqs=6, max_pages_per_seq=8, device=DEV)
+        pool.extend([0], [n])
+        pool.append(0, [0], [n], *rows)
+        pool.truncate([0], [keep])
+        pool.fork([0], [1])
+        pools.append(pool)
+    q = torch.randn(2, 24, D, generator=g).to(DEV)
+    qm = torch.randn(2, 3, 24, D, generator=g).to(DEV)
+
+    def same(fn):
+        for a, b in zip(*(fn(p) for p in pools)):
+            assert torch.isfinite(a).all() and torch.equal(a, b)
+    same(lambda p: p.decode(0, [0, 1], q))
+    same(lambda p: p.decode_multi(0, [0, 1], qm[:, :min(3, keep)].contiguous()))
+    same(lambda p: p.decode_multi(0, [0, 1], qm[:, :2].contiguous()))
+    one = [torch.randn(2, H, D, generator=g).to(DEV) for _ in range(2)]
+    for p in pools:
+        p.extend([0, 1], [1, 1])
+    same(lambda p: p.append_decode(0, [0, 1], *one, q))
+    same(lambda p: p.dequantize(0, 1, 0, p.seq_info(1)[1]))
+    # the freed pages' next owner
+    few = [torch.randn(5, H, D, generator=g).to(DEV) for _ in range(2)]
+    for p in pools:
+        p.extend([0], [6])                                # the rows of old values come into use again: written anew
+        p.append(0, [0], [6], *(torch.cat([x, x[:1]]) for x in few))
+        p.release(0)
+        p.release(1)
+        p.extend([2], [P + 5])
+        p.append(0, [2], [P + 5], torch.cat([k[:1].expand(P, H, D), few[0]]), torch.cat([v[:1].expand(P, H, D), few[1]]))
+    same(lambda p: p.decode(0, [2], q[:1]))
+    for p in pools:
+        p.check_device_errors()
