@@ -317,9 +317,10 @@ typedef struct {
  * device array [tokens] of int32 or int64 (position_bytes 4 or 8); head_dim
  * from rot_dim to 4096, at most 4096 heads.  dtype MKV_F32, MKV_BF16 or MKV_F16.
  * transpose != 0 applies the transpose of the map (the gradient of q and k given
- * those of the outputs; with m = 1 also its inverse).  Enqueued on `stream`.  Errors: INVALID_ARGUMENT
- * (NULL, sizes, dtype, strides of an output that overlap, in place with other
- * strides, addresses not aligned to the element). */
+ * those of the outputs; with m = 1 also its inverse).  Neither output may overlap
+ * the other tensor's rows.  Enqueued on `stream`.  Errors: INVALID_ARGUMENT (NULL,
+ * sizes, dtype, strides of an output that overlap, in place with other strides,
+ * addresses not aligned to the element). */
 mkv_status mkv_rope(const mkv_rope_table* table, int64_t tokens, int32_t head_dim, const void* positions,
                     int32_t position_bytes, const mkv_rope_rows* q, const mkv_rope_rows* k, mkv_dtype dtype,
                     int32_t transpose, mkv_stream_t stream);
@@ -329,7 +330,7 @@ mkv_status mkv_rope(const mkv_rope_table* table, int64_t tokens, int32_t head_di
  * at their token's position in its sequence (0 for the first) and quantised
  * from the fp32 result; V rows are quantised as they are; q (may be NULL, with
  * q_out) [sum n_new, H_q, d] is rotated at the same positions into q_out
- * (q_out == q allowed).  q, k, v and q_out are contiguous, of one dtype
+ * (q_out == q allowed; else it overlaps none of the inputs).  q, k, v and q_out are contiguous, of one dtype
  * (MKV_F32 or MKV_BF16) and 16-byte aligned.  Errors: those of
  * mkv_append_tokens, INVALID_ARGUMENT for the table or the alignment, device
  * and capture as mkv_seq_fork (a step under a graph: mkv_rope in it, then the
@@ -382,7 +383,8 @@ mkv_status mkv_decode_attention(mkv_pool* pool, int32_t layer, int32_t n, const 
  * go in pairs: the plan holds n * ceil(nq / 2) batch entries, entry
  * b * ceil(nq / 2) + j reading request b's prefix up to its query token
  * min(2j + 1, nq - 1) for query tokens 2j and 2j + 1 together (each block is
- * dequantised once for both; token 2j masks the prefix's last token).
+ * dequantised once for both; token 2j masks the prefix's last token, by weight 0:
+ * a NaN or an infinity in its V reaches both).
  * Errors: those of mkv_decode_attention; INVALID_ARGUMENT for
  * nq < 1, n * nq > max_batch or a sequence shorter than nq; INVALID_STATE
  * when a query token sits in a TQ3 page. */

@@ -50,11 +50,11 @@
 // of 14,584 with heads of 128 16.9 -> 15.2, the ragged batch 305 -> 297 .. 300).  The next piece's query rows are split
 // behind this piece's first tile, not before it, where they delayed every CTA's first softmax by 5,000 cycles.
 //
-// Measured (HBM copy rate 6,695 GB/s): 64 requests of 1,024 .. 65,536 tokens, 32 / 8 heads of 128, bf16: 297 .. 300 us
-// for 2.02 GB, the copy rate.  8 requests of 8K .. 32K, four query tokens, 24 / 4 heads of 256, fp16: 63.2 us
-// for 314 MB (74 %); of 64K and 128K each: 171 and 326 us (94 and 98 %), so long calls are bound by memory and some
-// 20 us are the start (cold code, the first codes), the pieces' ends and the join; 12 us for one query token.  One
-// request of 4,096: 12.3 us, that latency alone.
+// Measured (HBM copy rate 6,695 GB/s): 64 requests of 1,024 .. 65,536 tokens, 32 / 8 heads of 128, bf16: 305 .. 308 us
+// for 2.02 GB, 98 % (297 with two parts a weight).  8 requests of 8K .. 32K, four query tokens, 24 / 4 heads of 256,
+// fp16: 65.5 us for 314 MB (72 %; 63 with three parts); of 64K and 128K each: 168 and 323 us (95 and 99 %), so long
+// calls are bound by memory and some 20 us are the start (cold code, the first codes), the pieces' ends and the join; 12 us
+// for one query token.  One request of 4,096: 12.5 us, that latency alone.
 // Tried and not kept: tiles drawn from a counter in chunks (the ragged batch 316 us, the 8 requests 108: every change
 // of piece costs about four tiles); QK and PV issued by two warps (the ragged batch 327 us); whole runs of page ids
 // fetched ahead (330: a faster mean, a slower last CTA).
